@@ -82,6 +82,13 @@ __device__ __forceinline__ float glr_cap(float a, float cap) {
     return r;
 }
 
+// max(a, low) that keeps a NaN
+__device__ __forceinline__ float glr_floor(float a, float low) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(low));
+    return r;
+}
+
 // e^-s of the argument -s (fp32 io) or -s log2(e) (bf16 io, the
 // single-instruction exponential; with fp32 io its error would add up over a
 // long memory, and expf and the rounded reciprocal are used).  kGlrScale turns
@@ -122,22 +129,30 @@ __device__ __forceinline__ void sigmoid2(float2 arg, float2& f, float2& w) {
     w = __fmul2_rn(e, f);
 }
 
-// The same for the forget gate (f, w) and the output gate (g, n) of a token
-// with one reciprocal for both: the kernels run into the rate of the
-// multi-function unit, 3 instead of 4 of its instructions per element.  A NaN
-// must not cross over: the output gate's argument drops its NaN (silu
-// multiplies by z, which has it), and a NaN forget gate makes NaN only what it
+// The same for the forget gate (f, w) and the output gate (g, n) of a token, and
+// silu(z) = z g, with one reciprocal for both: the kernels run into the rate of the
+// multi-function unit, 3 instead of 4 of its instructions per element.  The
+// output gate's 1 + e is held times 2^-124, so that e can go up to 2^124 and the
+// product of both denominators still has a reciprocal; below that z, the
+// product takes the z where e has reached it: silu(z) is then -86 x 2^-124, and not
+// z times a g that has stopped falling (4 x 4096 x 4096 forward 110 us, with e^-|z|
+// and selections, which go on to 0, 113 us).
+// A NaN must not cross over: the output gate's argument drops its NaN (the
+// product with z has it), and a NaN forget gate makes NaN only what it
 // makes NaN anyway, the token's state and what follows from it.
 template <typename T>
-__device__ __forceinline__ void sigmoid2_both(float2 arg, float2 argz, float2& f, float2& w, float2& g, float2& n) {
+__device__ __forceinline__ void sigmoid2_both(float2 arg, float2 z, float2& f, float2& w, float2& g, float2& n, float2& silu) {
+    constexpr float kTop = 124.f / (sizeof(T) == 2 ? 1.f : kLog2e), kScaled = 0x1p-124f;
+    const float2 argz = __fmul2_rn(z, splat(kGlrScale<T>));
     const float2 e = glr_exp<T>(make_float2(glr_cap(arg.x, kGlrCap<T>), glr_cap(arg.y, kGlrCap<T>)));
-    const float2 ez = glr_exp<T>(make_float2(fminf(argz.x, kGlrCap<T>), fminf(argz.y, kGlrCap<T>)));
-    const float2 d = __fadd2_rn(e, splat(1.f)), dz = __fadd2_rn(ez, splat(1.f));
+    const float2 ez = glr_exp<T>(make_float2(fminf(argz.x, kTop), fminf(argz.y, kTop)));
+    const float2 d = __fadd2_rn(e, splat(1.f)), dz = __ffma2_rn(ez, splat(kScaled), splat(kScaled));
     const float2 r = glr_rcp<T>(__fmul2_rn(d, dz));
     f = glr_refine(__fmul2_rn(r, dz), d);
-    g = __fmul2_rn(r, d);
     w = __fmul2_rn(e, f);
+    g = __fmul2_rn(__fmul2_rn(r, d), splat(kScaled));
     n = __fmul2_rn(ez, g);
+    silu = __fmul2_rn(make_float2(glr_floor(z.x, kTop / kGlrScale<T>), glr_floor(z.y, kTop / kGlrScale<T>)), g);
 }
 
 // A lane's two channels of one token, in shared and in global memory.
@@ -616,10 +631,8 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
         const auto gates = [&](int i) {
             const float2 arg = __ffma2_rn(get(0, i), splat(kGlrScale<T>), bias);
             if constexpr (kZ) {
-                const float2 z = get(kArrays - 1, i);
-                float2 n;
-                sigmoid2_both<T>(arg, __fmul2_rn(z, splat(kGlrScale<T>)), f[i], v[i], g[i], n);
-                g[i] = __fmul2_rn(z, g[i]);
+                float2 sg, sn;
+                sigmoid2_both<T>(arg, get(kArrays - 1, i), f[i], v[i], sg, sn, g[i]);
             } else {
                 sigmoid2<T>(arg, f[i], v[i]);
             }
@@ -793,10 +806,8 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
             if constexpr (!kZ) {
                 sigmoid2<T>(arg, f[i], w[i]);
             } else {
-                const float2 z = get(kArrays - 1, i);
-                float2 sg, sn;
-                sigmoid2_both<T>(arg, __fmul2_rn(z, splat(kGlrScale<T>)), f[i], w[i], sg, sn);
-                const float2 si = __fmul2_rn(z, sg);
+                float2 sg, sn, si;
+                sigmoid2_both<T>(arg, get(kArrays - 1, i), f[i], w[i], sg, sn, si);
                 v[i] = __fmul2_rn(u[i], __ffma2_rn(si, sn, sg));
                 u[i] = __fmul2_rn(u[i], si);
             }
@@ -975,11 +986,9 @@ __global__ void glr_update_kernel(const float* state, float* state_out, const T*
             // a single channel rides along twice
             const int k = i + 1 < kN ? i + 1 : i;
             const float2 arg = make_float2(fmaf(vg.get(i), kGlrScale<T>, bv[i]), fmaf(vg.get(k), kGlrScale<T>, bv[k]));
-            float2 f, w, out = splat(1.f), n;
+            float2 f, w, g, n, out = splat(1.f);
             if (z) {
-                const float2 zz = make_float2(vz.get(i), vz.get(k));
-                sigmoid2_both<T>(arg, __fmul2_rn(zz, splat(kGlrScale<T>)), f, w, out, n);
-                out = __fmul2_rn(zz, out);
+                sigmoid2_both<T>(arg, make_float2(vz.get(i), vz.get(k)), f, w, g, n, out);
             } else {
                 sigmoid2<T>(arg, f, w);
             }
