@@ -549,7 +549,8 @@ MSS_API int mss_state_update_conv(float *state, void *conv_state, const void *x,
  * It is mss_scan_fwd's recurrence under MSS_FLAG_ZOH_INPUT at dstate 1 with
  * A = -1, B = C = 1, no D and delta = -s_t: exp(-softplus(v)) = sigmoid(-v).  1 - f_t
  * is formed as the sigmoid of -s_t, so it keeps its precision where f_t is near 1.
- * sigmoid(z) is held at 2^-124 or more: silu(z) of z below -86 is about -4e-36.
+ * f_t and sigmoid(z) are held at 2^-124 or more (s_t and z of about -86): a gate
+ * below that leaves 5e-38 of the state before it, and silu(z) is about -4e-36.
  *
  *   x, gate, z, y : [batch][seqlen][dim] dtype, token-major like mss_ssd_fwd
  *                   (z may be NULL)

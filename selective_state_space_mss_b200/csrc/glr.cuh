@@ -92,11 +92,11 @@ __device__ __forceinline__ float glr_floor(float a, float low) {
 // e^-s of the argument -s (fp32 io) or -s log2(e) (bf16 io, the
 // single-instruction exponential; with fp32 io its error would add up over a
 // long memory, and expf and the rounded reciprocal are used).  kGlrScale turns
-// a gate into the argument.  Capped at 2^60, about: see below.
+// a gate into the argument.  Capped at 2^124, which leaves 1 + e a reciprocal.
 template <typename T> constexpr float kGlrScale = -1.f;
 template <> constexpr float kGlrScale<bf16_t> = -kLog2e;
-template <typename T> constexpr float kGlrCap = 41.f;
-template <> constexpr float kGlrCap<bf16_t> = 60.f;
+template <typename T> constexpr float kGlrCap = 124.f / kLog2e;
+template <> constexpr float kGlrCap<bf16_t> = 124.f;
 
 template <typename T>
 __device__ __forceinline__ float2 glr_exp(float2 a) {
@@ -119,7 +119,7 @@ __device__ __forceinline__ float2 glr_refine(float2 f, float2 d) {
 
 // f = sigmoid(s) = 1 / (1 + e) and w = 1 - f = e / (1 + e) with e = e^-s: no
 // subtraction, so both keep their precision.  The cap on e keeps w finite and
-// f at least 2^-60 (of a state that 1 - f has just replaced).
+// f at least 2^-124.
 template <typename T>
 __device__ __forceinline__ void sigmoid2(float2 arg, float2& f, float2& w) {
     const float2 e = glr_exp<T>(make_float2(glr_cap(arg.x, kGlrCap<T>), glr_cap(arg.y, kGlrCap<T>)));
@@ -132,27 +132,27 @@ __device__ __forceinline__ void sigmoid2(float2 arg, float2& f, float2& w) {
 // The same for the forget gate (f, w) and the output gate (g, n) of a token, and
 // silu(z) = z g, with one reciprocal for both: the kernels run into the rate of the
 // multi-function unit, 3 instead of 4 of its instructions per element.  The
-// output gate's 1 + e is held times 2^-124, so that e can go up to 2^124 and the
-// product of both denominators still has a reciprocal; below that z, the
-// product takes the z where e has reached it: silu(z) is then -86 x 2^-124, and not
-// z times a g that has stopped falling (4 x 4096 x 4096 forward 110 us, with e^-|z|
+// output gate's 1 + e is held times 2^-124, so that the product of both
+// denominators has a reciprocal although either e goes up to 2^124.  Below the z
+// where e has reached its cap the product takes that z: silu(z) is then -86 x 2^-124,
+// and not z times a g that has stopped falling (4 x 4096 x 4096 forward 110 us, with e^-|z|
 // and selections, which go on to 0, 113 us).
 // A NaN must not cross over: the output gate's argument drops its NaN (the
 // product with z has it), and a NaN forget gate makes NaN only what it
 // makes NaN anyway, the token's state and what follows from it.
 template <typename T>
 __device__ __forceinline__ void sigmoid2_both(float2 arg, float2 z, float2& f, float2& w, float2& g, float2& n, float2& silu) {
-    constexpr float kTop = 124.f / (sizeof(T) == 2 ? 1.f : kLog2e), kScaled = 0x1p-124f;
+    constexpr float kScaled = 0x1p-124f, kLowest = kGlrCap<T> / kGlrScale<T>;
     const float2 argz = __fmul2_rn(z, splat(kGlrScale<T>));
     const float2 e = glr_exp<T>(make_float2(glr_cap(arg.x, kGlrCap<T>), glr_cap(arg.y, kGlrCap<T>)));
-    const float2 ez = glr_exp<T>(make_float2(fminf(argz.x, kTop), fminf(argz.y, kTop)));
+    const float2 ez = glr_exp<T>(make_float2(fminf(argz.x, kGlrCap<T>), fminf(argz.y, kGlrCap<T>)));
     const float2 d = __fadd2_rn(e, splat(1.f)), dz = __ffma2_rn(ez, splat(kScaled), splat(kScaled));
     const float2 r = glr_rcp<T>(__fmul2_rn(d, dz));
     f = glr_refine(__fmul2_rn(r, dz), d);
     w = __fmul2_rn(e, f);
     g = __fmul2_rn(__fmul2_rn(r, d), splat(kScaled));
     n = __fmul2_rn(ez, g);
-    silu = __fmul2_rn(make_float2(glr_floor(z.x, kTop / kGlrScale<T>), glr_floor(z.y, kTop / kGlrScale<T>)), g);
+    silu = __fmul2_rn(make_float2(glr_floor(z.x, kLowest), glr_floor(z.y, kLowest)), g);
 }
 
 // A lane's two channels of one token, in shared and in global memory.

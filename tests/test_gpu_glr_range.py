@@ -145,3 +145,16 @@ def test_output_gate(values, form, dt):
     """silu goes to 0 below, to z above, and so do the gradients through it."""
     d, g = _inputs(dt, 150, None, values[:form[0]], 1.0, 3)
     _check(d, g, dt, form[1])
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=IDS)
+@pytest.mark.parametrize("form", FORMS, ids=["tma", "pieces", "elements"])
+@pytest.mark.parametrize("z", ["none", "plain", "extreme"])
+@pytest.mark.parametrize("size", [1.0, 1e12, 1e25])
+@pytest.mark.parametrize("values", [BELOW, ABOVE + BELOW[9:16]], ids=["low", "high"])
+def test_forget_gate(values, size, z, form, dt):
+    """A state of any size is replaced where the gate says so, and held where it says that."""
+    n = form[0]
+    zs = dict(none=None, plain=[], extreme=(BELOW[::-1])[:n])[z]
+    d, g = _inputs(dt, 150, values[:n], zs, size, 5)
+    _check(d, g, dt, form[1])
