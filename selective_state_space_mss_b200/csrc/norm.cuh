@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
         const S* s = static_cast<const S*>(p.x) + r * p.dim;
         const T* dy = static_cast<const T*>(p.dy) + r * p.dim;
         const S* dres = p.residual ? static_cast<const S*>(p.residual) + r * p.dim : nullptr;
-        const float rstd = next_rstd, center = -next_mean * next_rstd;
+        const float rstd = next_rstd, mean = next_mean;
         fetch(r + stride);
         const S* const s_in = s;
         const T* const dy_in = dy;
@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
             if (!kRing && dres) add[j] = q.load(dres);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                hat[j].v[i] = kMean ? __ffma2_rn(hat[j].v[i], both(rstd), both(center)) : __fmul2_rn(hat[j].v[i], both(rstd));
+                // the difference first: -mean rstd rounded would not cancel where the mean is far above the spread
+                if (kMean) hat[j].v[i] = __fadd2_rn(hat[j].v[i], both(-mean));
+                hat[j].v[i] = __fmul2_rn(hat[j].v[i], both(rstd));
                 dw[j].v[i] = __ffma2_rn(g[j].v[i], hat[j].v[i], dw[j].v[i]);
                 if (kMean) db[j].v[i] = __fadd2_rn(db[j].v[i], g[j].v[i]);
                 g[j].v[i] = __fmul2_rn(g[j].v[i], w[j].v[i]);
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
         if (edge) {
             const float d = loose ? ld(dy_in + ec) : ld(dy + ec);
             ehat = loose ? ld(s_in + ec) : ld(s + ec);
-            ehat = kMean ? fmaf(ehat, rstd, center) : ehat * rstd;
+            ehat = (kMean ? ehat - mean : ehat) * rstd;
             edw = fmaf(d, ehat, edw);
             edb += d;
             eg = d * ew;
