@@ -35,6 +35,7 @@
 
 #include "mss_device.cuh"
 #include "mss_params.h"
+#include "ring.h"
 #include "tma.cuh"
 
 namespace mss {
@@ -507,10 +508,7 @@ struct GlrRing {
     // After a wait that gave up: waits once more for the boxes in flight.
     __device__ __forceinline__ void drain(const GlrParams& p) {
         if constexpr (kTma) {
-            for (int i = 0; i < kStages; ++i) {
-                mbar_wait_bounded(bar + slot, parity, p.err);
-                if (++slot == kStages) slot = 0, parity ^= 1;
-            }
+            drain_ring(slot, parity, kStages, kStages, [&](int, int at, uint32_t phase) { mbar_wait_bounded(bar + at, phase, p.err); });
         } else {
             asm volatile("cp.async.wait_all;" ::: "memory");
         }

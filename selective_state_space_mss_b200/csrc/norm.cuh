@@ -21,6 +21,7 @@
 
 #include "mss_device.cuh"
 #include "mss_params.h"
+#include "ring.h"
 #include "tma.cuh"
 
 namespace mss {
@@ -382,10 +383,9 @@ __global__ void __launch_bounds__(kNormRingThreads<kPieces>) norm_fwd_ring_kerne
         const float rstd = 1.f / sqrtf(total(sum.x + sum.y, part[2 + buf]) * inv + p.eps);
         // the whole group has read the slot
         if (gave_up[buf][group]) {  // no more copies; those in flight are waited for
-            for (int k = 1; k < stages; ++k) {
-                if (++slot == stages) slot = 0, parity ^= 1;
-                if (r + k * stride < p.rows) mbar_wait_bounded(bar + slot, parity, p.err);
-            }
+            drain_ring(slot, parity, stages, stages, [&](int k, int at, uint32_t phase) {
+                if (r + k * stride < p.rows) mbar_wait_bounded(bar + at, phase, p.err);
+            });
             break;
         }
         if (t == 0) issue(slot, r + stages * stride);
@@ -547,12 +547,10 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
             __syncwarp();
         }
         if (kRing) {  // the whole group is done with the slot of the row before
-            if (gave_up[buf][group]) {  // no more copies; those in flight are waited for
-                const int ahead = used < 0 ? stages : stages - 1;
-                for (int k = 1; k < ahead; ++k) {
-                    if (++slot == stages) slot = 0, parity ^= 1;
-                    if (r + k * stride < p.rows) mbar_wait_bounded(bar + slot, parity, p.err);
-                }
+            if (gave_up[buf][group]) {  // no more copies; those in flight are waited for (`used` is not filled anew yet)
+                drain_ring(slot, parity, stages, used < 0 ? stages : stages - 1, [&](int k, int at, uint32_t phase) {
+                    if (r + k * stride < p.rows) mbar_wait_bounded(bar + at, phase, p.err);
+                });
                 break;
             }
             if (t == 0 && used >= 0) issue(used, r + (stages - 1) * stride);
