@@ -724,9 +724,10 @@ MSS_API int64_t mss_norm_bwd_workspace_size(int64_t rows, int64_t dim);
  * device error word that kernels set when a bounded wait gives up
  * (MSS_ERR_DEVICE_TIMEOUT) or packed offsets break their rule
  * (MSS_ERR_OFFSETS), or MSS_ERR_CUDA if the stream itself reports an
- * error.  Returns MSS_OK when neither happened.  The error word is one
- * word of device memory per device, defined in the library image; nothing
- * is allocated.
+ * error.  Returns MSS_OK when neither happened.  Where both did, the first call
+ * reports and clears the timeout and the next one the offsets.  The error word
+ * is one word of device memory per device, defined in the library image;
+ * nothing is allocated.
  */
 MSS_API int mss_get_device_error(void *stream);
 

@@ -937,6 +937,7 @@ def probe_pipe_rates(stream=None, device=None) -> dict:
 
 def get_device_error(stream=None, device=None) -> int:
     """Synchronise the stream and return (and clear) the library's device
-    error status: 0, or a negative mss_status code."""
+    error status: 0, or a negative mss_status code (ERR_DEVICE_TIMEOUT before
+    ERR_OFFSETS, one a call)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     return int(load_library().mss_get_device_error(_stream_handle(stream, dev)))

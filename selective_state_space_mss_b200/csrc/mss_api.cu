@@ -29,6 +29,10 @@ constexpr unsigned kBwdFlags = MSS_FLAG_GENERAL_A | MSS_FLAG_SIMPLE | MSS_FLAG_Z
 // parameter block; mss_get_device_error reads and clears it.
 __device__ unsigned int g_mss_device_error = 0u;
 
+// One bit of it, so that what kernels of this or another stream set beside it
+// or in the meantime is still to be reported.
+__global__ void clear_device_error(unsigned int bit) { atomicAnd(&g_mss_device_error, ~bit); }
+
 // Address of a __device__ symbol on the current device, looked up once.
 template <typename Symbol>
 void* symbol_address(const Symbol& sym, void* (&cache)[kMaxDevices], std::mutex& mu) {
@@ -575,19 +579,16 @@ int mss_ssd_fwd_ex2(const void* x, const void* dt, const float* A, const void* B
 int mss_get_device_error(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return MSS_ERR_CUDA;
-    unsigned int word = 0, zero = 0;
+    unsigned int word = 0;
     if (cudaMemcpyFromSymbolAsync(&word, g_mss_device_error, sizeof(word), 0,
                                   cudaMemcpyDeviceToHost, s) != cudaSuccess)
         return MSS_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return MSS_ERR_CUDA;
-    if (word != 0) {
-        if (cudaMemcpyToSymbolAsync(g_mss_device_error, &zero, sizeof(zero), 0,
-                                    cudaMemcpyHostToDevice, s) != cudaSuccess ||
-            cudaStreamSynchronize(s) != cudaSuccess)
-            return MSS_ERR_CUDA;
-        return word & mss::kDeviceErrTimeout ? MSS_ERR_DEVICE_TIMEOUT : MSS_ERR_OFFSETS;
-    }
-    return MSS_OK;
+    if (word == 0) return MSS_OK;
+    const unsigned int told = word & mss::kDeviceErrTimeout ? mss::kDeviceErrTimeout : mss::kDeviceErrOffsets;
+    clear_device_error<<<1, 1, 0, s>>>(told);
+    if (launch_status() != MSS_OK || cudaStreamSynchronize(s) != cudaSuccess) return MSS_ERR_CUDA;
+    return told == mss::kDeviceErrTimeout ? MSS_ERR_DEVICE_TIMEOUT : MSS_ERR_OFFSETS;
 }
 
 }  // extern "C"
