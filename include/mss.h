@@ -678,6 +678,7 @@ MSS_API int mss_glr_update(float *state, float *state_out, const void *x, const 
  * The statistics are those of the rounded s, taken in fp32 in two passes over
  * the row in registers (the mean, then the centred squares).  eps must be >= 0
  * and finite (MSS_ERR_SHAPE).  Any sizes; 16-byte aligned rows take wide loads.
+ * rows == 0 or dim == 0 writes nothing, mean and rstd included.
  */
 MSS_API int mss_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias, float eps,
                          void *y, void *residual_out, float *mean, float *rstd, int64_t rows, int64_t dim,

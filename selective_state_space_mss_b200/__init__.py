@@ -832,7 +832,8 @@ def norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, rms=False, y=None, r
     root-mean-square form), mean and rstd None with want_stats=False.
 
     x: [..., dim] float32 or bfloat16; weight, bias: [dim] float32; residual,
-    residual_out: [..., dim] float32 or x's type; mean, rstd: [...] float32."""
+    residual_out: [..., dim] float32 or x's type; mean, rstd: [...] float32 (NaN
+    for rows without elements)."""
     if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
         raise ValueError("x must be a CUDA tensor (there is no CPU path)")
     if x.dim() < 1:
@@ -864,6 +865,11 @@ def norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, rms=False, y=None, r
     _on_device(dev, stream, "mss_norm_fwd", _addr(x), _addr(residual), _addr(weight), _addr(bias),
                float(eps), _addr(y), _addr(residual_out), _addr(mean), _addr(rstd), rows, dim, code,
                DTYPE_F32 if rdt == torch.float32 else DTYPE_BF16, NORM_FLAG_RMS if rms else 0)
+    if dim == 0 and want_stats:  # 0 / 0: the library writes nothing for rows without elements
+        with torch.cuda.stream(stream):
+            for v in (mean, rstd):
+                if v is not None:
+                    v.fill_(float("nan"))
     return y, residual_out, mean, rstd
 
 
