@@ -58,7 +58,7 @@
 extern "C" {
 #endif
 
-#define MSS_VERSION 10600 /* major*10000 + minor*100 + patch: 1.6.0 */
+#define MSS_VERSION 10700 /* major*10000 + minor*100 + patch: 1.7.0 */
 
 enum mss_dtype {
     MSS_DTYPE_F32 = 0,
@@ -719,6 +719,21 @@ MSS_API int mss_norm_bwd(const void *s, const float *weight, const float *mean, 
 
 /* Workspace bytes mss_norm_bwd needs with dweight or dbias, or MSS_ERR_SHAPE. */
 MSS_API int64_t mss_norm_bwd_workspace_size(int64_t rows, int64_t dim);
+
+/*
+ * mss_selftest_timeout -- self-test of the bounded waits of mss_glr_fwd,
+ * mss_glr_bwd, mss_norm_fwd and mss_norm_bwd (for tests of the failure path;
+ * MSS_FLAG_SELFTEST_TIMEOUT is that of the scan).  From a call with on != 0 to
+ * the next with 0, what this host thread launches of them waits for its first
+ * tiles or rows with a limit of 1 ms, and their barriers count an arrival more
+ * than the copies make, which comes only when those waits have given up.  The
+ * device error word is set and the kernels return behind the late arrivals;
+ * outputs and workspace are unspecified, nothing else is written, and the CUDA
+ * context stays usable.
+ * Meanwhile calls whose sizes and alignments take a kernel without such waits
+ * return MSS_ERR_FLAGS and launch nothing.  Returns the setting before (0 or 1).
+ */
+MSS_API int mss_selftest_timeout(int on);
 
 /*
  * mss_get_device_error -- synchronises `stream`, then reports and clears the

@@ -30,7 +30,7 @@ import torch
 __all__ = ["scan_fwd", "scan_fwd_host", "scan_fwd_conv", "scan_bwd", "ssd_fwd", "bwd_workspace_size", "state_update", "state_update_conv",
            "glr_fwd", "glr_fwd_save", "glr_bwd", "glr_bwd_workspace_size", "glr_update",
            "norm_fwd", "norm_bwd", "norm_bwd_workspace_size",
-           "get_device_error", "probe_pipe_rates",
+           "get_device_error", "probe_pipe_rates", "selftest_timeout",
            "library_path", "workspace_size",
            "FLAG_GENERAL_A", "FLAG_SIMPLE", "FLAG_NO_SPLIT", "FLAG_ZOH_INPUT", "FLAG_SELFTEST_TIMEOUT",
            "ERR_DEVICE_TIMEOUT", "ERR_FLAGS", "ERR_OFFSETS", "SSD_FLAG_WARP_MMA", "MssError", "load_library"]
@@ -146,6 +146,8 @@ def load_library():
             lib.mss_norm_bwd.restype = i
             lib.mss_norm_bwd_workspace_size.argtypes = [i64, i64]
             lib.mss_norm_bwd_workspace_size.restype = i64
+            lib.mss_selftest_timeout.argtypes = [i]
+            lib.mss_selftest_timeout.restype = i
             lib.mss_get_device_error.argtypes = [vp]
             lib.mss_get_device_error.restype = i
             lib.mss_strerror.argtypes = [i]
@@ -939,6 +941,14 @@ def probe_pipe_rates(stream=None, device=None) -> dict:
     if rc != 0:
         raise MssError(rc, "mss_probe_pipe_rates")
     return {k: float(v) for k, v in zip(PIPE_RATE_NAMES, out)}
+
+
+def selftest_timeout(on: bool) -> bool:
+    """Self-test of the bounded waits of the recurrence and the norm
+    (mss_selftest_timeout): while on, this thread's calls give up waiting after
+    1 ms and set the device error status; their outputs are then unspecified.
+    Returns the setting before."""
+    return bool(load_library().mss_selftest_timeout(1 if on else 0))
 
 
 def get_device_error(stream=None, device=None) -> int:

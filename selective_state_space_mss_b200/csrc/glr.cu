@@ -172,6 +172,9 @@ int launch_glr(GlrParams p, bool bwd, int64_t units, int* cluster, cudaStream_t 
     constexpr int64_t kMaxCoordinate = int64_t(1) << 31;
     const bool tma = p.pairs > 0 && p.dim * esz % 16 == 0 && p.batch < kMaxCoordinate &&
                      p.seqlen < kMaxCoordinate - mss::kGlrTile && p.dim < kMaxCoordinate - mss::kGlrCols;
+    p.wait_ns = wait_limit_ns();
+    p.selftest = selftest_timeout();
+    if (p.selftest && !tma) return MSS_ERR_FLAGS;  // no waits for tiles to test
     *cluster = tma ? glr_cluster<T, true>(bwd, units, p.seqlen) : glr_cluster<T, false>(bwd, units, p.seqlen);
     mss::GlrMaps maps{};
     if (tma && (!encode_glr(&maps.gate, p.gate, p, esz) || !encode_glr(&maps.x, p.x, p, esz) ||

@@ -497,7 +497,7 @@ struct GlrRing {
     // The tile in the current slot has arrived; false when its wait gave up.
     __device__ __forceinline__ bool wait(const GlrParams& p) {
         if constexpr (kTma) {
-            return mbar_wait_bounded(bar + slot, parity, p.err);
+            return mbar_wait_bounded(bar + slot, parity, p.err, p.wait_ns);
         } else {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
@@ -508,7 +508,10 @@ struct GlrRing {
     // After a wait that gave up: waits once more for the boxes in flight.
     __device__ __forceinline__ void drain(const GlrParams& p) {
         if constexpr (kTma) {
-            drain_ring(slot, parity, kStages, kStages, [&](int, int at, uint32_t phase) { mbar_wait_bounded(bar + at, phase, p.err); });
+            drain_ring(slot, parity, kStages, kStages, [&](int, int at, uint32_t phase) {
+                if (p.selftest && (threadIdx.x & 31) == 0) mbar_arrive(bar + at);  // what the wait was for comes late
+                mbar_wait_bounded(bar + at, phase, p.err);
+            });
         } else {
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
         gave_up = stop = 0;
         mbar_init(slot_bar, 1);
         mbar_init(slot_bar + 1, 1);
-        for (int i = 0; i < kGlrWarps * kStages; ++i) mbar_init(&full[0][0] + i, 1);
+        for (int i = 0; i < kGlrWarps * kStages; ++i) mbar_init(&full[0][0] + i, 1 + p.selftest);
         fence_barrier_init();
     }
     __syncthreads();
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
         gave_up = stop = 0;
         mbar_init(slot_bar, 1);
         mbar_init(slot_bar + 1, 1);
-        for (int i = 0; i < kGlrWarps * kStages; ++i) mbar_init(&full[0][0] + i, 1);
+        for (int i = 0; i < kGlrWarps * kStages; ++i) mbar_init(&full[0][0] + i, 1 + p.selftest);
         fence_barrier_init();
     }
     __syncthreads();

@@ -16,6 +16,12 @@ namespace mss_host {
 // null when the lookup fails.
 unsigned int* device_error_word();
 
+// What mss_selftest_timeout has set for this thread.
+bool selftest_timeout();
+
+// A bounded wait's limit: 2 s, in the self-test 1 ms.
+inline unsigned long long wait_limit_ns() { return selftest_timeout() ? 1000000ull : 2000000000ull; }
+
 // Forward pass over validated arguments (p.err set): picks the throughput
 // kernel or the scalar one and, with a workspace, the sequence split.
 template <typename T, int N>

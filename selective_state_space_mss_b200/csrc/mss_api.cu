@@ -51,6 +51,9 @@ void* symbol_address(const Symbol& sym, void* (&cache)[kMaxDevices], std::mutex&
 
 namespace mss_host {
 
+thread_local bool t_selftest_timeout = false;
+bool selftest_timeout() { return t_selftest_timeout; }
+
 unsigned int* device_error_word() {
     static std::mutex mu;
     static void* cache[kMaxDevices] = {};
@@ -574,6 +577,12 @@ int mss_ssd_fwd_ex2(const void* x, const void* dt, const float* A, const void* B
         if (rc != MSS_OK || chunked0 == pairs) return rc;
     }
     return launch_ssd_chunked(p, int(dstate), workspace, chunked0, pairs - chunked0, s);
+}
+
+int mss_selftest_timeout(int on) {
+    const int before = t_selftest_timeout;
+    t_selftest_timeout = on != 0;
+    return before;
 }
 
 int mss_get_device_error(void* stream) {

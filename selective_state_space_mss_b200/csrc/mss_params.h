@@ -133,6 +133,8 @@ struct GlrParams {
     float* states;            // [batch, ceil(seqlen / 64), dim]: written by the forward pass (may be null), read by the backward pass
     int64_t batch, seqlen, dim, nseq;
     unsigned int* err;        // device error word
+    unsigned long long wait_ns;  // limit of a wait for a tile
+    int selftest;             // 1: a tile is there only with an arrival that comes after the wait gave up (mss_selftest_timeout)
     int pairs;                // 1: dim is even and the io tensors are aligned to two elements; -1: an input does
                               // not begin on 16 bytes; else 0
     // backward pass
@@ -161,6 +163,8 @@ struct NormParams {
     float eps;
     int rms;
     unsigned int* err;        // device error word
+    unsigned long long wait_ns;  // limit of a wait for a row
+    int selftest;             // as in GlrParams
 };
 
 }  // namespace mss

@@ -82,6 +82,7 @@ int run_norm_fwd(const NormParams& p, bool wide, bool aligned, cudaStream_t s) {
     // 1001 4.6 against 4.2 us.
     if (!wide && aligned && p.dim <= 8192)
         return p.dim <= 256 ? launch_norm_fwd_ring<T, R, 1>(p, s) : launch_norm_fwd_ring<T, R, 2>(p, s);
+    if (p.selftest) return MSS_ERR_FLAGS;  // no waits for rows to test
     const NormShape sh = norm_fwd_shape(p.rows, p.dim, wide);
     if (sh.G > 1024 || p.rows > 0x7fffffffLL)
         mss::norm_fwd_long_kernel<T, R><<<unsigned(std::min<int64_t>(p.rows, 148 * 8)), 256, 0, s>>>(p);
@@ -131,6 +132,7 @@ int launch_norm_bwd(const NormParams& p, int64_t* blocks, cudaStream_t s) {
 
 template <typename T, typename S>
 int run_norm_bwd(const NormParams& p, mss::NormRows rows, bool mean, int64_t* blocks, cudaStream_t s) {
+    if (p.selftest && (p.dim > 8192 || rows == mss::kRowsStrided)) return MSS_ERR_FLAGS;  // no waits for rows to test
     if (p.dim > 8192) {
         mss::norm_bwd_long_kernel<T, S><<<unsigned(*blocks), 512, 0, s>>>(p);
         return launch_status();
@@ -180,6 +182,7 @@ int mss_norm_fwd(const void* x, const void* residual, const float* weight, const
     NormParams p{};
     p.x = x, p.residual = residual, p.weight = weight, p.bias = bias, p.y = y, p.residual_out = residual_out;
     p.mean = mean, p.rstd = rstd, p.rows = rows, p.dim = dim, p.eps = eps, p.rms = (flags & MSS_NORM_FLAG_RMS) != 0;
+    p.wait_ns = wait_limit_ns(), p.selftest = selftest_timeout();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool begins = all_aligned(io, 16) && all_aligned(rs, 16);
     const bool wide = begins && dim % 8 == 0 && aligned(weight, 16) && aligned(bias, 16);
@@ -220,6 +223,7 @@ int mss_norm_bwd(const void* s_in, const float* weight, const float* mean, const
     p.x = s_in, p.weight = weight, p.mean = const_cast<float*>(mean), p.rstd = const_cast<float*>(rstd), p.dy = dy;
     p.residual = dresidual_out, p.y = dx, p.residual_out = dresidual, p.rows = rows, p.dim = dim;
     p.part = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    p.wait_ns = wait_limit_ns(), p.selftest = selftest_timeout();
     if (!(p.err = device_error_word())) return MSS_ERR_CUDA;
     const mss::NormRows lie = !all_aligned(io, 16) || !all_aligned(ss, 16) ? mss::kRowsStrided
                               : dim % 8 == 0 && aligned(weight, 16)       ? mss::kRowsWide

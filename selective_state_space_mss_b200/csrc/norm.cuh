@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kNormRingThreads<kPieces>) norm_fwd_ring_kerne
     };
     if (t == 0) {
         gave_up[0][group] = gave_up[1][group] = 0;
-        for (int k = 0; k < stages; ++k) mbar_init(bar + k, 1);
+        for (int k = 0; k < stages; ++k) mbar_init(bar + k, 1 + p.selftest);
         fence_barrier_init();
     }
     __syncthreads();
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kNormRingThreads<kPieces>) norm_fwd_ring_kerne
         const T* x = reinterpret_cast<const T*>(ring + slot * slot_bytes) + shift;
         const R* res = reinterpret_cast<const R*>(ring + slot * slot_bytes + tb) + shift;
         R* out = p.residual_out ? static_cast<R*>(p.residual_out) + r * p.dim : nullptr;
-        if (!mbar_wait_bounded(bar + slot, parity, p.err)) gave_up[buf][group] = 1;
+        if (!mbar_wait_bounded(bar + slot, parity, p.err, p.wait_ns)) gave_up[buf][group] = 1;
         Octet s[kPieces];
         float2 sum = both(0.f);
 #pragma unroll
@@ -384,7 +384,9 @@ __global__ void __launch_bounds__(kNormRingThreads<kPieces>) norm_fwd_ring_kerne
         // the whole group has read the slot
         if (gave_up[buf][group]) {  // no more copies; those in flight are waited for
             drain_ring(slot, parity, stages, stages, [&](int k, int at, uint32_t phase) {
-                if (r + k * stride < p.rows) mbar_wait_bounded(bar + at, phase, p.err);
+                if (r + k * stride >= p.rows) return;
+                if (p.selftest && t == 0) mbar_arrive(bar + at);  // what the wait was for comes late
+                mbar_wait_bounded(bar + at, phase, p.err);
             });
             break;
         }
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
     if (kRing) {
         if (t == 0) {
             gave_up[0][group] = gave_up[1][group] = 0;
-            for (int k = 0; k < stages; ++k) mbar_init(bar + k, 1);
+            for (int k = 0; k < stages; ++k) mbar_init(bar + k, 1 + p.selftest);
             fence_barrier_init();
         }
         __syncthreads();
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
             s = reinterpret_cast<const S*>(ring + slot * slot_bytes) + shift;
             dy = reinterpret_cast<const T*>(ring + slot * slot_bytes + sb) + shift;
             if (dres) dres = reinterpret_cast<const S*>(ring + slot * slot_bytes + sb + tb) + shift;
-            if (!mbar_wait_bounded(bar + slot, parity, p.err)) gave_up[buf][group] = 1;
+            if (!mbar_wait_bounded(bar + slot, parity, p.err, p.wait_ns)) gave_up[buf][group] = 1;
         }
         Octet hat[kPieces], g[kPieces];
         typename Piece<kRows>::template Held<S> add[kRing ? 1 : kPieces];
@@ -549,7 +551,9 @@ __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(
         if (kRing) {  // the whole group is done with the slot of the row before
             if (gave_up[buf][group]) {  // no more copies; those in flight are waited for (`used` is not filled anew yet)
                 drain_ring(slot, parity, stages, used < 0 ? stages : stages - 1, [&](int k, int at, uint32_t phase) {
-                    if (r + k * stride < p.rows) mbar_wait_bounded(bar + at, phase, p.err);
+                    if (r + k * stride >= p.rows) return;
+                    if (p.selftest && t == 0) mbar_arrive(bar + at);  // what the wait was for comes late
+                    mbar_wait_bounded(bar + at, phase, p.err);
                 });
                 break;
             }

@@ -19,3 +19,20 @@ def test_every_copy_in_flight_is_waited_for(tmp_path):
     assert build.returncode == 0, build.stderr
     run = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert run.returncode == 0 and run.stdout.strip() == "ok", run.stdout + run.stderr
+
+
+def test_the_self_test_is_a_setting_of_the_thread():
+    """Also what a call refuses comes first: no launch, no device."""
+    import threading
+
+    import selective_state_space_mss_b200 as mss
+    from selective_state_space_mss_b200 import build as mss_build
+
+    mss_build.build()
+    seen = []
+    assert mss.selftest_timeout(True) is False and mss.selftest_timeout(True) is True
+    t = threading.Thread(target=lambda: seen.append(mss.selftest_timeout(False)))
+    t.start()
+    t.join()
+    assert seen == [False]
+    assert mss.selftest_timeout(False) is True and mss.selftest_timeout(False) is False
