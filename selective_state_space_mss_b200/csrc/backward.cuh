@@ -30,16 +30,12 @@ int64_t backward_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen, uns
 template <typename T, int N>
 bool encode_ckpt(CUtensorMap* m, const void* base, int64_t rows, int64_t seqlen) {
     using Ly = mss::BwdLayout<T, N>;
-    auto enc = encode_tiled_fn();
-    if (!enc) return false;
     const int64_t width = seqlen / Ly::kVec * N;
     const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(width * 4)};
     const cuuint32_t box[2] = {cuuint32_t(Ly::kGroups * N), cuuint32_t(Ly::kRows)};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename T, int N, bool kGate, bool kSoftplus, bool kZoh>

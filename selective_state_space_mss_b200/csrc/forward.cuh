@@ -10,7 +10,6 @@
 #include <mutex>
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "host_common.h"
@@ -18,50 +17,26 @@
 #include "scan_seq.cuh"
 #include "scan_seq4.cuh"
 #include "scan_simple.cuh"
+#include "tensor_map.h"
 
 namespace mss_host {
 
-// cuTensorMapEncodeTiled, resolved once through the runtime so that the
-// library does not link the driver library itself.
-inline PFN_cuTensorMapEncodeTiled_v12000 encode_tiled_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
 // [rows, L] row-major view, box = box_rows rows x 128 bytes, 128-byte swizzle.
 inline bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t L, int esz, int box_rows) {
-    auto enc = encode_tiled_fn();
-    if (!enc) return false;
     const cuuint64_t dims[2] = {cuuint64_t(L), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(L * esz)};
     const cuuint32_t box[2] = {cuuint32_t(128 / esz), cuuint32_t(box_rows)};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return enc(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // [batch, N, L] view, box = 1 x N x 128 bytes, no swizzle.
 inline bool encode_bc(CUtensorMap* m, const void* base, int64_t batch, int64_t N, int64_t L, int esz) {
-    auto enc = encode_tiled_fn();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {cuuint64_t(L), cuuint64_t(N), cuuint64_t(batch)};
     const cuuint64_t strides[2] = {cuuint64_t(L * esz), cuuint64_t(N * L * esz)};
     const cuuint32_t box[3] = {cuuint32_t(128 / esz), cuuint32_t(N), 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename T, int N>

@@ -3,32 +3,18 @@
 #include <algorithm>
 #include <iterator>
 
-#include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
-
 #include "host_common.h"
 #include "launch.h"
 
 #include "glr.cuh"
 #include "sum_rows.cuh"
+#include "tensor_map.h"
 
 namespace mss_host {
 namespace {
 
 using mss::bf16_t;
 using mss::GlrParams;
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
 
 // Sizes in bytes of one call's arrays; false on a negative size or overflow.
 struct GlrSizes {
@@ -57,16 +43,11 @@ int copy_or_zero(float* dst, const float* src, int64_t bytes, cudaStream_t s) {
 // channels behind the end read as zero.
 bool encode_glr(CUtensorMap* m, const void* base, const GlrParams& p, int esz) {
     if (!base) return true;
-    auto enc = encode_tiled_fn();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {cuuint64_t(p.dim), cuuint64_t(p.seqlen), cuuint64_t(p.batch)};
     const cuuint64_t strides[2] = {cuuint64_t(p.dim * esz), cuuint64_t(p.seqlen * p.dim * esz)};
     const cuuint32_t box[3] = {cuuint32_t(mss::kGlrCols), cuuint32_t(mss::kGlrRun), 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename T, bool kTma, bool kPacked, bool kZ>

@@ -4,7 +4,6 @@
 #include <mutex>
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "host_common.h"
@@ -12,37 +11,21 @@
 #include "ssd_chunked.cuh"
 #include "ssd_mma.cuh"
 #include "ssd_tc.cuh"
+#include "tensor_map.h"
 
 namespace mss_host {
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 ssd_encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
 // [batch][L][n1][n0] bf16 as a 4-D view (n0 innermost); box = 64 x 1 x 128 x 1
 // (128 tokens of 64 elements), 128-byte swizzle.  Tokens past L read as zero
 // and are not written by stores.
 bool encode_token_major(CUtensorMap* m, const void* base, int64_t batch, int64_t L, int64_t n1, int64_t n0) {
-    auto enc = ssd_encode_fn();
-    if (!enc) return false;
     const cuuint64_t dims[4] = {cuuint64_t(n0), cuuint64_t(n1), cuuint64_t(L), cuuint64_t(batch)};
     const cuuint64_t strides[3] = {cuuint64_t(n0 * 2), cuuint64_t(n1 * n0 * 2), cuuint64_t(L * n1 * n0 * 2)};
     const cuuint32_t box[4] = {64u, 1u, 128u, 1u};
-    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <bool kGate, bool kSoftplus>
