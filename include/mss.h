@@ -551,6 +551,8 @@ MSS_API int mss_state_update_conv(float *state, void *conv_state, const void *x,
  * is formed as the sigmoid of -s_t, so it keeps its precision where f_t is near 1.
  * f_t and sigmoid(z) are held at 2^-124 or more (s_t and z of about -86): a gate
  * below that leaves 5e-38 of the state before it, and silu(z) is about -4e-36.
+ * An infinity or NaN makes what follows it in its sequence and channel infinite or
+ * NaN, and nothing else.
  *
  *   x, gate, z, y : [batch][seqlen][dim] dtype, token-major like mss_ssd_fwd
  *                   (z may be NULL)
@@ -647,6 +649,8 @@ MSS_API int64_t mss_glr_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_
  *   x, gate, z : [batch][dim] dtype (z may be NULL)
  *   gate_bias  : [dim] float (NULL: 0)
  *   y          : [batch][dim] dtype output
+ *
+ * Errors: MSS_ERR_DTYPE, _SHAPE, _NULL, _ALIGN, _ALIAS, _CUDA.
  */
 MSS_API int mss_glr_update(float *state, float *state_out, const void *x, const void *gate, const void *z,
                            const float *gate_bias, void *y, int64_t batch, int64_t dim, int dtype, void *stream);
@@ -676,9 +680,13 @@ MSS_API int mss_glr_update(float *state, float *state_out, const void *x, const 
  *                  residual_out is given (else MSS_ERR_DTYPE)
  *
  * The statistics are those of the rounded s, taken in fp32 in two passes over
- * the row in registers (the mean, then the centred squares).  eps must be >= 0
- * and finite (MSS_ERR_SHAPE).  Any sizes; 16-byte aligned rows take wide loads.
- * rows == 0 or dim == 0 writes nothing, mean and rstd included.
+ * the row (the mean, then the centred squares, whose sum must not pass fp32's range).
+ * Any sizes; 16-byte aligned rows take wide loads, and rows of up to 16384
+ * elements are read once.  rows == 0 or dim == 0 writes nothing, mean and rstd
+ * included.  No output may overlap an input (residual_out not residual either) or
+ * another output.
+ * Errors: MSS_ERR_FLAGS, _DTYPE, _SHAPE (also eps < 0, infinite or NaN), _NULL,
+ * _ALIGN, _ALIAS, _CUDA.
  */
 MSS_API int mss_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias, float eps,
                          void *y, void *residual_out, float *mean, float *rstd, int64_t rows, int64_t dim,
@@ -709,8 +717,11 @@ MSS_API int mss_norm_fwd(const void *x, const void *residual, const float *weigh
  *                   with dweight or dbias.  Calls that share a workspace must not
  *                   overlap in time.
  *
- * The sums over rows are taken in fp32 in a fixed order: results are bitwise
- * reproducible.  rows == 0 writes dweight = dbias = 0.
+ * The sums over rows are taken in fp32 in a fixed order, at most about rows / 144 +
+ * 45 additions one behind another: results are bitwise reproducible.  rows == 0
+ * writes dweight = dbias = 0.  Rows past 8192 elements take a kernel several times
+ * slower.  No output may overlap an input, another output or the workspace.
+ * Errors: MSS_ERR_DTYPE, _SHAPE, _NULL, _ALIGN, _WORKSPACE, _ALIAS, _CUDA.
  */
 MSS_API int mss_norm_bwd(const void *s, const float *weight, const float *mean, const float *rstd, const void *dy,
                          const void *dresidual_out, void *dx, void *dresidual, float *dweight, float *dbias,

@@ -835,7 +835,8 @@ def norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, rms=False, y=None, r
 
     x: [..., dim] float32 or bfloat16; weight, bias: [dim] float32; residual,
     residual_out: [..., dim] float32 or x's type; mean, rstd: [...] float32 (NaN
-    for rows without elements)."""
+    for rows without elements).  No output may be an input's memory, residual_out
+    not residual's either."""
     if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
         raise ValueError("x must be a CUDA tensor (there is no CPU path)")
     if x.dim() < 1:

@@ -91,10 +91,10 @@ cudaLaunchConfig_t glr_config(cudaLaunchAttribute* at, int64_t units, int cluste
 }
 
 // Blocks that share the sequence of one unit (64 channels of a batch row): the
-// most that still run all units at once and all have a tile.  Measured for 1
-// x 12288 x 1536 (24 units): 10 blocks 51 us, 8 57 us, 12 (two rounds) 70 us;
-// 2 x 8192 x 2560 (80 units): 3 blocks 94 us, 2 131 us, 4 118 us; 1 x 65536 x
-// 256 (4 units): 16 blocks 125 us, 8 216 us.
+// most that still run all units at once and all have a tile.  Measured (bf16
+// forward, with z) for 1 x 12288 x 1536 (24 units): 10 blocks 48 us, 8 53 us, 12
+// (two rounds) 66 us; 2 x 8192 x 2560 (80 units): 3 blocks 92 us, 2 128 us, 4 113
+// us; 1 x 65536 x 256 (4 units): 16 blocks 120 us, 8 205 us.
 constexpr int kGlrClusters[] = {16, 14, 12, 10, 9, 8, 7, 6, 5, 4, 3, 2};
 constexpr int64_t kGlrBlocks = 2 * 148;  // at most two blocks per SM of a B200 run at once
 

@@ -50,8 +50,8 @@ constexpr int kGlrMaxCluster = 16;
 
 // Slots of a ring.  fp32 boxes are twice as large: where two slots would leave
 // an SM one block instead of two, one slot and the other block's work hide the
-// loads better (1 x 3001 x 1001 fp32 forward: 22.5 against 30.6 us, backward
-// 33.6 against 40.0 us).
+// loads better (1 x 3001 x 1001 fp32 with z forward: 24 against 31 us, backward
+// 36 against 44 us; 4 x 4096 x 4096 fp32 backward 331 against 395 us).
 template <typename T, bool kTma, bool kBwd> constexpr int kGlrStages = sizeof(T) == 4 && (kBwd || !kTma) ? 1 : 2;
 constexpr int kGlrSlotBytes = 32 * 16;              // a block's pair of each of its channels
 
@@ -554,10 +554,10 @@ __device__ __forceinline__ float2 glr_row(const Place& me, const GlrParams& p, c
 // The kernels.  Two blocks of eight warps per SM: a third would leave a thread 80
 // registers, too few for eight tokens of two channels.
 
-// Bound by memory: 8 bytes per element (bf16, with z).  4 x 4096 x 4096: 107 us, 5.0
+// Bound by memory: 8 bytes per element (bf16, with z).  4 x 4096 x 4096: 110 us, 4.9
 // TB/s.  In clusters the exchange between a tile's two barriers costs a fifth: 1
-// x 131072 x 2048, 9 blocks a cluster, 532 us, 4.0 TB/s.  Packed sequences with 37
-// borders in 12289 x 1536: 53 us, without borders 46 us, the dense kernel 38 us.
+// x 131072 x 2048, 9 blocks a cluster, 541 us, 4.0 TB/s.  12289 x 1536 without z:
+// the dense kernel 38 us, the packed one 46 us with one sequence and 53 us with 37.
 template <typename T, bool kTma, bool kPacked, bool kZ>
 __global__ void __launch_bounds__(kGlrThreads, 2)
     glr_fwd_kernel(const __grid_constant__ GlrMaps maps, const GlrParams p) {
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kGlrThreads, 2)
 // the states from the saved one, the gradients from behind.  The states are run
 // through again in place of being kept for the second loop, which would cost
 // 16 registers.  Bound by memory, 14 bytes per element (bf16, with z): 4 x 4096 x
-// 4096 in 184 us, 5.1 TB/s.
+// 4096 in 188 us, 5.0 TB/s.
 template <typename T, bool kTma, bool kPacked, bool kZ>
 __global__ void __launch_bounds__(kGlrThreads, 2)
     glr_bwd_kernel(const __grid_constant__ GlrMaps maps, const GlrParams p) {

@@ -125,7 +125,7 @@ int launch_norm_bwd(const NormParams& p, int64_t* blocks, cudaStream_t s) {
     // One piece a thread where a warp takes the row, else two, which halve the work per
     // row that is not per element; with fp32 rows of middle length the memory sets
     // the time and one piece leaves more loads in flight.  16384 x 1024 bf16: two
-    // 29, one 32 us; fp32: 47 both; 16384 x 1531 fp32: 79, 70 us.
+    // 31, one 38 us; fp32: 47 both; 16384 x 1531 fp32: 78, 73 us.
     if (pieces <= 32 || (sizeof(S) == 4 && pieces > 64 && pieces <= 288)) return launch_norm_bwd<T, S, kRows, kMean, 1>(p, group(1), blocks, s);
     return launch_norm_bwd<T, S, kRows, kMean, 2>(p, group(2), blocks, s);
 }

@@ -5,7 +5,7 @@
 //
 // Bound by memory: every element is read and written once, with a few
 // operations between, so a row is kept in the registers of the threads that
-// share it -- a group of one to 24 warps.
+// share it -- a group of one to 32 warps (backward 16).
 //
 // Rows of whole 16-byte words are taken word by word.  Other rows begin anywhere
 // in a word, but all tensors are dense and flat element k lies in the word that
@@ -31,10 +31,11 @@ constexpr int kNormGroups = 18;  // groups of a block at most; 15 where they nee
 // How the rows lie: whole 16-byte words, parts of them behind aligned addresses,
 // or anything.
 enum NormRows { kRowsWide, kRowsShifted, kRowsStrided };
-// Threads of a block of the backward pass at most.  One piece a thread and wide
-// rows: 576 leave the registers that 768 would spill (16384 x 768: 38 against 44
-// us); strided loads need the threads of 768 (16384 x 1023: 80 against 89
-// us).
+// Threads of a block of the backward pass at most.  One piece a thread through
+// the ring: 576 leave the registers that 768 would spill (16384 x 768: 38 against 44
+// us).  Strided loads, which tensors take that begin between words, need the
+// threads of 768 although they spill (16384 x 1023 bf16 with a fp32 residual: 91 against
+// 122 us).
 template <int kRows, int kPieces> constexpr int kNormThreads = kPieces == 2 ? 512 : kRows == kRowsStrided ? 768 : 576;
 
 // Eight elements of a row as four pairs, for packed two-wide arithmetic.
@@ -267,8 +268,8 @@ template <int kPieces> constexpr int kNormRingThreads = kPieces == 2 ? 640 : 768
 // Forward pass over rows that begin anywhere in a word: as the backward pass
 // below, each group of G threads takes every (blocks * groups)-th row, streamed
 // through a ring in shared memory, and keeps its columns' weight and bias in
-// registers.  16384 x 1023 bf16 with a fp32 residual: 37 us,
-// 5.4 TB/s (by strides: 66 us); 1003 x 769 fp32 4.8 us.
+// registers.  16384 x 1023 bf16 with a fp32 residual: 38 us,
+// 5.3 TB/s (by strides: 67 us); 1003 x 769 fp32 4.8 us.
 template <typename T, typename R, int kPieces>
 __global__ void __launch_bounds__(kNormRingThreads<kPieces>) norm_fwd_ring_kernel(const NormParams p, int G, int stages) {
     extern __shared__ __align__(128) unsigned char ring_mem[];
@@ -416,9 +417,9 @@ __global__ void __launch_bounds__(kNormRingThreads<kPieces>) norm_fwd_ring_kerne
 // registers of two pieces; a slot is filled anew once the whole group has come to
 // the sums of the next row.  kRowsShifted: gridDim.x * groups * dim is a multiple of 8, or every group
 // has one row.
-// kMean: with avg(g) and dbias.  With the sum over the blocks, 16384 x 2048 bf16: 49
-// us, 5.6 TB/s; 16384 x 768 with a fp32 residual: 38 us, 5.3 TB/s; 16384 x 1023: 54
-// us, 5.0 TB/s (strided: 79 us).
+// kMean: with avg(g) and dbias.  With the sum over the blocks, 16384 x 2048 bf16: 48
+// us, 5.6 TB/s; 16384 x 768 with a fp32 residual: 38 us, 5.3 TB/s; 16384 x 1023: 55
+// us, 4.9 TB/s (strided: 91 us).
 template <typename T, typename S, int kRows, bool kMean, int kPieces>
 __global__ void __launch_bounds__(kNormThreads<kRows, kPieces>) norm_bwd_kernel(const NormParams p, int G, int stages) {
     extern __shared__ __align__(128) unsigned char ring_mem[];
@@ -633,7 +634,8 @@ __device__ __forceinline__ float norm_input(const T* x, const R* res, int64_t i)
     return res ? to_f32(from_f32<R>(v + ld(res + i))) : v;
 }
 
-// One block per row, any length: the row is read three times.
+// Rows past 16384 elements, one block per row: the row is read three times
+// (2048 x 20000 bf16 with a fp32 residual 328 us, 1.5 TB/s).
 template <typename T, typename R>
 __global__ void norm_fwd_long_kernel(const NormParams p) {
     __shared__ float tmp[32];
@@ -665,8 +667,10 @@ __global__ void norm_fwd_long_kernel(const NormParams p) {
     }
 }
 
-// A block takes every gridDim.x-th row; its sums for dweight and dbias stay in
-// its own row of the partial sums, each column in one thread's hands.
+// Rows past 8192 elements.  A block takes every gridDim.x-th row; its sums for
+// dweight and dbias stay in its own row of the partial sums, each column in one
+// thread's hands.  Element loads, and the sums go through memory with every row:
+// 4096 x 12288 bf16 with a fp32 residual 852 us, 0.9 TB/s (8192 columns, in registers: 4.4).
 template <typename T, typename S>
 __global__ void norm_bwd_long_kernel(const NormParams p) {
     __shared__ float tmp[32];
